@@ -20,8 +20,10 @@
  *   - the calls keep no state between them: any number may run at the same time, on any
  *     streams (moe_linear_backward: each with a workspace of its own);
  *   - results do not depend on timing: no atomics, sums in a fixed order;
- *   - all sums are held in fp32; a bf16 result is rounded once, at the end, except the
- *     gradient dz of moe_linear_backward, which is rounded to bf16 between its two products;
+ *   - all sums are held in fp32 (bf16 products on the tensor cores, which cut off below 2^-23
+ *     of the running sum, in parts of at most 16384 terms: within 2^-13 of the sum of the
+ *     terms' magnitudes, however many there are); a bf16 result is rounded once, at the end, except
+ *     the gradient dz of moe_linear_backward, which is rounded to bf16 between its two products;
  *   - the return value reports argument validation and launch errors; errors found on the
  *     device (offsets out of range, a bounded wait that timed out) go to a per-device status
  *     word that moe_ops_check_status() reads and clears.

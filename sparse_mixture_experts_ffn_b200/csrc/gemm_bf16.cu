@@ -48,6 +48,13 @@ constexpr int kPatchWarp = 10;
 constexpr int kABytes = kM * kL * 2;
 constexpr int kChunkBytes = kL * 64 * 2;  // an MN-major box: 64 reduction steps x 64 elements
 constexpr int kCols = 32;                 // columns per epilogue chunk
+// Stages that one accumulator sums.  The tensor cores cut off, not round, what does not fit at every
+// addition of 16 steps, so an accumulator's error grows with its length and all one way: up to
+// 2^-23 an addition, 2^-13 for these 1024, a 32nd of half a step of bf16.  Longer sums are shared out
+// evenly over parts of at most so many stages, added in fp32 (equal terms: in one accumulator,
+// 300000 rows were off by 1.6e-3 more than half a step, 10^6 rows by 9.6e-3).  A part costs its tile
+// 1 us; parts of 128 stages would cost 4096 x 4096 x 11264 3%.
+constexpr int kPart = 256;
 constexpr int kMaxSmem = 232448;
 
 // Shared memory of the epilogue's two groups of warps, each: buffers for chunks of 32 columns on
@@ -355,6 +362,43 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
                : "memory");
 }
 
+// the inverse of tmem_ld16_nowait(), and the wait for this thread's stores
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+      "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// parts of a sum of nk stages, and the first stage of part i
+__device__ __forceinline__ int parts_of(int nk) { return (nk + kPart - 1) / kPart; }
+__device__ __forceinline__ int part_begin(int nk, int i, int parts) {
+  return static_cast<int>(static_cast<int64_t>(nk) * i / parts);
+}
+
+// Adds an accumulator's columns to another's, one lane's row: `width` columns from `first` on, and
+// again every `turn`, as the calling warp will read them; SUMS accumulators, BN columns apart.
+template <int BN, int SUMS>
+__device__ __forceinline__ void add_part(uint32_t to, uint32_t from, int first, int width, int turn, int ncols) {
+  for (int c0 = first; c0 < ncols; c0 += turn)
+    for (int c = c0; c < min(c0 + width, ncols); c += 16)
+#pragma unroll 1
+      for (int a = 0; a < SUMS; ++a) {
+        uint32_t x[16], y[16];
+        float v[16];
+        tmem_ld16_nowait(to + c + a * BN, x);
+        tmem_ld16_nowait(from + c + a * BN, y);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(x[j]) + __uint_as_float(y[j]);
+        tmem_st16(to + c + a * BN, v);
+      }
+  tmem_wait_st();
+}
+
 // columns c .. c + 15 of a tile, one lane's row; BN = 16: the sum of its accumulators
 template <int BN>
 __device__ __forceinline__ void load_row16(uint32_t trow, int c, int sums, float* v) {
@@ -403,6 +447,14 @@ __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t* v) {
                : "memory");
 }
 
+// Chunks fetched from tensor memory at a time: a wait is for all fetches.  fwd keeps to one: its
+// activation's code is long.
+template <int PASS, int BN>
+constexpr int kFetched = PASS == kFwd || BN < 4 * kCols ? 1 : 2;
+// columns that a group of epilogue warps takes before the other's turn
+template <int PASS, int BN>
+constexpr int kTaken = kFetched<PASS, BN> * (BN < kCols ? 16 : 32);
+
 // one group of epilogue warps and its shared memory
 struct Group {
   int id;              // 0: warps 2 to 5, 1: warps 6 to 9
@@ -434,9 +486,7 @@ __device__ __forceinline__ void store_tile(const TcParams& p, const Tile& tile, 
                                            Group& grp, Ready ready, Release release) {
   constexpr int kHalves = BN < kCols ? 1 : 2;  // no column past the accumulator is read
   constexpr int kStep = 16 * kHalves;
-  // Chunks fetched from tensor memory at a time: a wait is for all fetches.  fwd keeps to one: its
-  // activation's code is long.
-  constexpr int kBlock = PASS == kFwd || BN < 4 * kCols ? 1 : 2;
+  constexpr int kBlock = kFetched<PASS, BN>;
   constexpr int kTurn = 2 * kBlock * kStep;  // columns of both groups' blocks
   const int et = (threadIdx.x - 64) & 127, lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3;
   const int group = et & 15, jr = et >> 4;  // ordinary stores: 8 features, every 8th column
@@ -817,23 +867,33 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
       const uint32_t sa = smem_u32(smem), sb = sa + kABytes;  // of stage 0
       Ring<C::kStages, C::kStageBytes> ring{full, empty, PASS == kFwd ? sw128_kmajor_desc(sa) : sw128_mnmajor_desc(sa),
                                             PASS == kWgrad ? sw128_mnmajor_desc(sb) : sw128_kmajor_desc(sb), 0, 0u, 0u};
-      int acc = 0;
-      uint32_t acc_phase = 0;
+      int acc = 0;        // accumulator of the tile's first part; further parts take the other one
+      uint32_t uses = 0;  // of each accumulator, modulo 2
+      bool ok = true;
       Walker<PASS, kM> walk(p, plan, first, step);
       Tile tile;
-      while (walk.next(tile)) {
+      while (ok && walk.next(tile)) {
         int kb0;
         const int nk = slice(tile.len, kb0);
         if (nk == 0) continue;  // the epilogue knows: nothing to add
         const uint32_t idesc = idesc_bf16_f32(kM, (tile.ncols + 15) & ~15) | major;
-        if (!wait_phase<false>(&tempty[acc], acc_phase ^ 1u, p.ctrl, abort_flag)) break;
-        tc_fence_after();
         const int left = min(kL, tile.len - (kb0 + nk - 1) * kL);
-        if (!mma_stages<PASS, false, C::kSums == 1 ? 0 : BN>(ring, nk, (left + 15) / 16, tmem_base + acc * C::kAccCols,
-                                                             idesc, left < kL ? pfull : nullptr, p.ctrl, abort_flag))
-          break;
-        mma_commit(&tfull[acc]);
-        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+        const int parts = parts_of(nk);
+        for (int i = 0; i < parts; ++i) {
+          const bool last = i + 1 == parts;
+          const int a = i ? acc ^ 1 : acc;
+          const int n = parts == 1 ? nk : part_begin(nk, i + 1, parts) - part_begin(nk, i, parts);
+          ok = wait_phase<false>(&tempty[a], ((uses >> a) & 1u) ^ 1u, p.ctrl, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          ok = mma_stages<PASS, false, C::kSums == 1 ? 0 : BN>(ring, n, last ? (left + 15) / 16 : kL / 16,
+                                                               tmem_base + a * C::kAccCols, idesc,
+                                                               last && left < kL ? pfull : nullptr, p.ctrl, abort_flag);
+          if (!ok) break;
+          mma_commit(&tfull[a]);
+          uses ^= 1u << a;
+        }
+        acc ^= 1;
       }
       mma_commit(drain);  // every MMA done before the accumulators are freed
       wait_phase<false>(drain, 0, p.ctrl, nullptr);
@@ -872,20 +932,34 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
     const int quarter = warp & 3;            // tensor-memory lanes this warp may read
     const int r = quarter * 32 + lane;       // feature of the tile
     int acc = 0, buf = 0;
-    uint32_t acc_phase = 0, buf_phase = 0;
+    uint32_t uses = 0, buf_phase = 0;
     bool failed = false;
     Walker<PASS, kM> walk(p, plan, first, step);
     Tile tile;
     while (walk.next(tile)) {
       int kb0;
       const int nk = slice(tile.len, kb0);
-      auto ready = [&] {
-        if (nk == 0) return;
-        if (!failed && !wait_phase<false>(&tfull[acc], acc_phase, p.ctrl, abort_flag)) failed = true;
+      const uint32_t trow0 = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+      const uint32_t trow = trow0 + acc * C::kAccCols;
+      auto finished = [&](int a) {  // waits for the products in accumulator a
+        if (!failed && !wait_phase<false>(&tfull[a], (uses >> a) & 1u, p.ctrl, abort_flag)) failed = true;
+        uses ^= 1u << a;
         __syncwarp();
         tc_fence_after();
       };
-      const uint32_t trow = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * C::kAccCols;
+      auto ready = [&] {
+        if (nk == 0) return;
+        finished(acc);
+        for (int i = 1; i < parts_of(nk); ++i) {
+          finished(acc ^ 1);
+          constexpr int kWidth = SPLIT ? BN : kTaken<PASS, BN>;
+          add_part<BN, C::kSums>(trow, trow0 + (acc ^ 1) * C::kAccCols, SPLIT ? 0 : grp.id * kWidth, kWidth,
+                                 SPLIT ? BN : 2 * kWidth, tile.ncols);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[acc ^ 1]);
+        }
+      };
       // accumulators written: one for each step of the first stage
       const int sums = nk == 0 ? 0 : C::kSums == 1 || nk > 1 ? C::kSums : (min(kL, tile.len - kb0 * kL) + 15) / 16;
       if constexpr (SPLIT) {
@@ -962,7 +1036,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
           if (lane == 0) mbar_arrive(&tempty[acc]);
         });
       }
-      if (nk && ++acc == 2) { acc = 0; acc_phase ^= 1u; }
+      if (nk) acc ^= 1;
     }
     bulk_wait();
   }
@@ -1113,22 +1187,31 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
       const uint32_t sa = smem_u32(smem), sb = sa + kABytes;  // of stage 0
       Ring<C::kStages, C::kStageBytes> ring{full, empty, PASS == kFwd ? sw128_kmajor_desc(sa) : sw128_mnmajor_desc(sa),
                                             PASS == kWgrad ? sw128_mnmajor_desc(sb) : sw128_kmajor_desc(sb), 0, 0u, 0u};
-      int acc = 0;
-      uint32_t acc_phase = 0;
+      int acc = 0;        // as in gemm_tc_kernel
+      uint32_t uses = 0;
+      bool ok = true;
       Walker<PASS, MT> walk(p, plan, first, step);
       Tile tile;
-      while (walk.next(tile)) {
+      while (ok && walk.next(tile)) {
         const int nk = (tile.len + kL - 1) / kL;
         if (nk == 0) continue;
         const uint32_t idesc = idesc_bf16_f32(MT, pair_columns(tile)) | major;
-        if (!wait_phase<true>(&tempty[acc], acc_phase ^ 1u, p.ctrl, abort_flag)) break;
-        tc_fence_after();
         const int left = tile.len - (nk - 1) * kL;
-        if (!mma_stages<PASS, true, 0>(ring, nk, (left + 15) / 16, tmem_base + acc * C::BN, idesc,
-                                    left < kL ? pfull : nullptr, p.ctrl, abort_flag))
-          break;
-        mma_commit_pair(&tfull[acc]);
-        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+        const int parts = parts_of(nk);
+        for (int i = 0; i < parts; ++i) {
+          const bool last = i + 1 == parts;
+          const int a = i ? acc ^ 1 : acc;
+          const int n = parts == 1 ? nk : part_begin(nk, i + 1, parts) - part_begin(nk, i, parts);
+          ok = wait_phase<true>(&tempty[a], ((uses >> a) & 1u) ^ 1u, p.ctrl, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          ok = mma_stages<PASS, true, 0>(ring, n, last ? (left + 15) / 16 : kL / 16, tmem_base + a * C::BN, idesc,
+                                         last && left < kL ? pfull : nullptr, p.ctrl, abort_flag);
+          if (!ok) break;
+          mma_commit_pair(&tfull[a]);
+          uses ^= 1u << a;
+        }
+        acc ^= 1;
       }
       mma_commit_pair(drain);  // every MMA done before the accumulators are freed
       wait_phase<false>(drain, 0, p.ctrl, nullptr);
@@ -1164,23 +1247,36 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
     grp.res = grp.pre + kChunk;
     grp.rbar = rbar + 2 * grp.id;
     int acc = 0;
-    uint32_t acc_phase = 0;
+    uint32_t uses = 0;
     bool failed = false;
     Walker<PASS, MT> walk(p, plan, first, step);
     Tile tile;
     while (walk.next(tile)) {
       const bool has = tile.len > 0;
-      auto ready = [&] {
-        if (!has) return;
-        if (!failed && !wait_phase<true>(&tfull[acc], acc_phase, p.ctrl, abort_flag)) failed = true;
+      const uint32_t trow0 = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+      const uint32_t trow = trow0 + acc * C::BN;
+      auto finished = [&](int a) {
+        if (!failed && !wait_phase<true>(&tfull[a], (uses >> a) & 1u, p.ctrl, abort_flag)) failed = true;
+        uses ^= 1u << a;
         __syncwarp();
         tc_fence_after();
       };
-      const uint32_t trow = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + acc * C::BN;
+      auto ready = [&] {
+        if (!has) return;
+        finished(acc);
+        for (int i = 1; i < parts_of((tile.len + kL - 1) / kL); ++i) {
+          finished(acc ^ 1);
+          constexpr int kWidth = kTaken<PASS, C::BN>;
+          add_part<C::BN, 1>(trow, trow0 + (acc ^ 1) * C::BN, grp.id * kWidth, kWidth, 2 * kWidth, tile.ncols);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(acc ? release0 : release1);
+        }
+      };
       store_tile<PASS, C::BN, FULL>(p, tile, tile.m0 + rank * kM, trow, has ? 1 : 0, grp, ready, [&] {
         if (lane == 0) mbar_arrive_remote(acc ? release1 : release0);
       });
-      if (has && ++acc == 2) { acc = 0; acc_phase ^= 1u; }
+      if (has) acc ^= 1;
     }
     bulk_wait();
   }

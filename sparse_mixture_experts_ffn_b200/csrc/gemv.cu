@@ -253,24 +253,42 @@ __global__ void __launch_bounds__(kMmaThreads, 2) gemv_bf16_kernel(const GemvPar
   };
   const int step = kChunk * p.ks;
   float c[4] = {};
+  // The tensor cores cut off what does not fit at each addition: sums of more than kPart turns (of 16
+  // additions each) are taken in parts and added in fp32, as in the tiles.
+  constexpr int kPart = 64;
 #pragma unroll
   for (int u = 0; u < kU; ++u) fetch(u, kw * kChunk + u * step);
-  for (int k0 = kw * kChunk; k0 < p.K; k0 += kU * step) {
+  for (int k0 = kw * kChunk, first = k0; k0 < p.K;) {
+    const int end = min(p.K, k0 + kPart * kU * step);
+    const bool again = k0 != first;
+    for (; k0 < end; k0 += kU * step) {
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int k = k0 + u * step;
-      uint4 b[2];  // from L1, except the first time
+      for (int u = 0; u < kU; ++u) {
+        const int k = k0 + u * step;
+        uint4 b[2];  // from L1, except the first time
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        b[h] = make_uint4(0, 0, 0, 0);
-        if (has && k + 32 * h + t * 8 < p.K) b[h] = __ldg(reinterpret_cast<const uint4*>(x + k + 32 * h));
+        for (int h = 0; h < 2; ++h) {
+          b[h] = make_uint4(0, 0, 0, 0);
+          if (has && k + 32 * h + t * 8 < p.K) b[h] = __ldg(reinterpret_cast<const uint4*>(x + k + 32 * h));
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          mma_16816(c, lo[u][h].x, hi[u][h].x, lo[u][h].y, hi[u][h].y, b[h].x, b[h].y);
+          mma_16816(c, lo[u][h].z, hi[u][h].z, lo[u][h].w, hi[u][h].w, b[h].z, b[h].w);
+        }
+        fetch(u, k + kU * step);
       }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        mma_16816(c, lo[u][h].x, hi[u][h].x, lo[u][h].y, hi[u][h].y, b[h].x, b[h].y);
-        mma_16816(c, lo[u][h].z, hi[u][h].z, lo[u][h].w, hi[u][h].w, b[h].z, b[h].w);
-      }
-      fetch(u, k + kU * step);
+    }
+    if (again) {  // the parts before, each lane's in a place of its own
+      const float4 s = part[warp][lane];
+      c[0] += s.x;
+      c[1] += s.y;
+      c[2] += s.z;
+      c[3] += s.w;
+    }
+    if (k0 < p.K) {
+      part[warp][lane] = make_float4(c[0], c[1], c[2], c[3]);
+      c[0] = c[1] = c[2] = c[3] = 0.0f;
     }
   }
   if (p.ks > 1) {
