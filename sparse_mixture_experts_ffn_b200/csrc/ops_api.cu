@@ -13,10 +13,22 @@
 namespace moe {
 namespace {
 
-// the status word of moe_ops_check_status(): one per device, zero when the library is loaded
-__device__ Ctrl g_ops_ctrl;
+// The status word of moe_ops_check_status(), one per device, zero when the library is loaded, and places
+// for what its checks took from it: each check has one of its own, as many as may run at a time.
+constexpr unsigned kChecks = 1024;
+struct OpsWord {
+  Ctrl ctrl;
+  int taken[kChecks];
+};
+__device__ OpsWord g_ops_word;
 
-Ctrl* ops_ctrl() {
+// Reads and clears the word in one step: what another stream's kernel records meanwhile is either
+// read now or left for the next check.
+__global__ void take_status_kernel(OpsWord* word, unsigned place) {
+  word->taken[place] = atomicExch(&word->ctrl.status, 0);
+}
+
+OpsWord* ops_word() {
   static std::atomic<void*> cache[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return nullptr;
@@ -25,12 +37,12 @@ Ctrl* ops_ctrl() {
     // the first use on a device may load the module, which a capture on this thread must not forbid
     cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
     cudaThreadExchangeStreamCaptureMode(&mode);
-    const cudaError_t e = cudaGetSymbolAddress(&p, g_ops_ctrl);
+    const cudaError_t e = cudaGetSymbolAddress(&p, g_ops_word);
     cudaThreadExchangeStreamCaptureMode(&mode);
     if (e != cudaSuccess) return nullptr;
     cache[dev].store(p, std::memory_order_release);
   }
-  return static_cast<Ctrl*>(p);
+  return static_cast<OpsWord*>(p);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -90,8 +102,9 @@ GemmArgs args_of(const moe_gemm_shape& s, GemmPass pass, const void* rows, const
 }
 
 moe_status run_gemm(const moe_gemm_shape& s, GemmArgs a, cudaStream_t st) {
-  a.ctrl = ops_ctrl();
-  if (!a.ctrl) return MOE_ERR_CUDA;
+  OpsWord* word = ops_word();
+  if (!word) return MOE_ERR_CUDA;
+  a.ctrl = &word->ctrl;
   const bool bf16 = s.dtype == MOE_BF16;
   const cudaError_t e = choose_gemv(a, bf16) ? launch_gemv(a, bf16, st) : bf16 ? launch_gemm_bf16(a, st) : launch_gemm_f32(a, st);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
@@ -262,11 +275,16 @@ extern "C" moe_status moe_swiglu_backward(int64_t R, int32_t I, int32_t dtype, c
 extern "C" moe_status moe_ops_check_status(void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (cudaStreamSynchronize(st) != cudaSuccess) return MOE_ERR_CUDA;
-  Ctrl* ctrl = ops_ctrl();
+  OpsWord* word = ops_word();
+  if (!word) return MOE_ERR_CUDA;
+  static std::atomic<unsigned> checks{0};
+  const unsigned place = checks.fetch_add(1, std::memory_order_relaxed) % kChecks;
   int status = 0;
-  if (!ctrl ||
-      cudaMemcpyAsync(&status, &ctrl->status, sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
-      cudaMemsetAsync(&ctrl->status, 0, sizeof(int), st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess)
+  count_launches(1);
+  take_status_kernel<<<1, 1, 0, st>>>(word, place);
+  if (cudaGetLastError() != cudaSuccess ||
+      cudaMemcpyAsync(&status, &word->taken[place], sizeof(int), cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+      cudaStreamSynchronize(st) != cudaSuccess)
     return MOE_ERR_CUDA;
   return static_cast<moe_status>(status);
 }
