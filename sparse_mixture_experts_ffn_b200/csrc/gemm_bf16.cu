@@ -652,8 +652,8 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 
-// What the copying thread has issued, so that after a failed wait it can let its copies land before
-// the block ends.
+// What the copying thread has issued, so that it can let its copies land before the block ends: also
+// when it has issued them all and another thread's wait failed.
 struct InFlight {
   uint32_t used = 0, partial = 0;    // per stage: used at all; its last use was a partial one
   uint32_t whole_odd = 0, part_odd = 0;  // per stage: uses of either kind so far, modulo 2
@@ -857,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
           if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
         }
       }
-      if (!ok) fly.land<C::kStages>(full, qfull, p.ctrl);
+      fly.land<C::kStages>(full, qfull, p.ctrl);
     }
   } else if (warp == 1) {
     // ------------------------------- MMAs ----------------------------------------------
@@ -1005,7 +1005,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_tc_kernel(const __grid_const
           for (int i = 0; i < kOwn; ++i)
             if (i < own) res[i] = p.residual[at0 + i * at_step];
         }
-        if (!failed && !wait_phase<true>(&rfull[buf], buf_phase, p.ctrl, abort_flag)) failed = true;
+        // (also after a failed wait: the blocks push all the same, and none may end before it has landed)
+        if (!wait_phase<true>(&rfull[buf], buf_phase, p.ctrl, nullptr)) failed = true;
         __syncwarp();
         float z[kOwn];
 #pragma unroll
@@ -1178,7 +1179,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemm_pair_kernel(const __grid_con
           if (++stage == C::kStages) { stage = 0; phase ^= 1u; }
         }
       }
-      if (!ok) fly.land<C::kStages>(rank == 0 ? full : nullptr, qfull, p.ctrl);
+      fly.land<C::kStages>(rank == 0 ? full : nullptr, qfull, p.ctrl);
     }
   } else if (warp == 1) {
     // ------------------------------- MMAs (even block) ---------------------------------
