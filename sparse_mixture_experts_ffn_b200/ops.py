@@ -6,7 +6,8 @@ devices are checked here (ValueError, before anything is launched), every sum ru
 library's CUDA kernels, and there is no fallback.  The calls run on the tensors' device, on its
 current stream unless ``stream`` is given (results not passed in are then allocated on that stream,
 and using them on another one needs the usual ordering); they record no autograd graph: a training
-loop calls the gradients itself.  A result that overlaps an input or another result is refused
+loop calls the gradients itself, and a tensor that requires grad is refused (ValueError) while grad
+mode is on, since its gradient would be lost.  A result that overlaps an input or another result is refused
 (MoEError), but for ``linear``'s y, which may be its residual.
 
     r = moe_layer_forward(x, W_router, ...)[1]          # routing: r.offsets, r.perm, r.topk_w
@@ -84,6 +85,15 @@ def _shape(R, N, K, E, code):
     return MoEGemmShape(R, N, K, E, code)
 
 
+def _no_graph(*tensors):
+    for t in tensors:
+        if t is not None and t.requires_grad:
+            import torch
+            if torch.is_grad_enabled():
+                raise ValueError("a tensor requires grad, and these calls record no graph: call them under "
+                                 "torch.no_grad() or on detached tensors, and the gradient functions yourself")
+
+
 def _cuda(t):
     if not t.is_cuda:
         raise ValueError("the tensors must be CUDA tensors (the operators run only on the GPU)")
@@ -135,6 +145,7 @@ def _grouped(entry, rows, W, offsets, out, out_name, stream, cols):
     shape = (R, N if cols == "N" else K)
     if out is not None:
         _check(out_name, out, rows.dtype, shape, dev)
+    _no_graph(rows, W)
     _cuda(rows)
     if out is None:
         out = _new(rows, shape, stream)
@@ -177,6 +188,7 @@ def grouped_gemm_wgrad(dy, x, offsets, *, dW=None, stream=None):
     _check("offsets", offsets, torch.int32, (E + 1,), dev)
     if dW is not None:
         _check("dW", dW, dy.dtype, (E, N, K), dev)
+    _no_graph(dy, x)
     _cuda(dy)
     if dW is None:
         dW = _new(dy, (E, N, K), stream)
@@ -218,6 +230,7 @@ def linear(x, W, *, bias=None, activation="none", residual=None, save_preact=Fal
         _check("y", y, dt, (R, N), dev)
     if preact is not None:
         _check("preact", preact, dt, (R, N), dev)
+    _no_graph(x, W, bias, residual)
     _cuda(x)
     if y is None:
         y = _new(x, (R, N), stream)
@@ -264,6 +277,7 @@ def linear_backward(dy, x, W, *, preact=None, activation="none", input_grad=True
     if workspace is not None and (workspace.device != dev or workspace.dtype != torch.uint8
                                   or not workspace.is_contiguous()):
         raise ValueError("workspace must be a contiguous uint8 tensor on dy's device")
+    _no_graph(dy, x, W, preact)
     _cuda(dy)
     if input_grad and dx is None:
         dx = _new(dy, (R, K), stream)
@@ -320,6 +334,7 @@ def swiglu(gate_up, *, row_w=None, limit=0.0, h=None, stream=None):
     code, R, I, dev, limit = _swiglu_args(gate_up, row_w, limit)
     if h is not None:
         _check("h", h, gate_up.dtype, (R, I), dev)
+    _no_graph(gate_up, row_w)
     _cuda(gate_up)
     if h is None:
         h = _new(gate_up, (R, I), stream)
@@ -339,6 +354,7 @@ def swiglu_backward(dh, gate_up, *, row_w=None, limit=0.0, d_gate_up=None, d_row
         if row_w is None:
             raise ValueError("d_row_w is given without row_w")
         _check("d_row_w", d_row_w, torch.float32, (R,), dev)
+    _no_graph(dh, gate_up, row_w)
     _cuda(gate_up)
     if d_gate_up is None:
         d_gate_up = _new(gate_up, (R, 2 * I), stream)

@@ -214,3 +214,29 @@ def test_sizes_that_would_wrap_in_32_bits_are_refused():
         with pytest.raises(ValueError, match="2\\^31"):
             call()
     assert moe.linear_backward_workspace_bytes(8, n, 8, BF, "silu", True) == 0
+
+
+@pytest.mark.parametrize("call", [
+    lambda t: moe.grouped_gemm(t(R, K), bf(E, N, K), offs()),
+    lambda t: moe.grouped_gemm(bf(R, K), t(E, N, K), offs()),
+    lambda t: moe.grouped_gemm_dgrad(t(R, N), bf(E, N, K), offs()),
+    lambda t: moe.grouped_gemm_wgrad(bf(R, N), t(R, K), offs()),
+    lambda t: moe.linear(bf(R, K), t(N, K)),
+    lambda t: moe.linear(bf(R, K), bf(N, K), bias=t(N, dtype=torch.float32)),
+    lambda t: moe.linear(bf(R, K), bf(N, K), residual=t(R, N)),
+    lambda t: moe.linear_backward(bf(R, N), bf(R, K), t(N, K)),
+    lambda t: moe.linear_backward(bf(R, N), bf(R, K), bf(N, K), preact=t(R, N), activation="silu"),
+    lambda t: moe.swiglu(t(R, 2 * N)),
+    lambda t: moe.swiglu(bf(R, 2 * N), row_w=t(R, dtype=torch.float32)),
+    lambda t: moe.swiglu_backward(t(R, N), bf(R, 2 * N)),
+])
+def test_tensors_that_require_grad_are_refused_while_grad_mode_is_on(call):
+    """The result would not require grad, and the gradient would be lost without a word."""
+    def leaf(*s, dtype=BF):
+        return torch.zeros(*s, dtype=dtype, requires_grad=True)
+    with pytest.raises(ValueError, match="requires grad"):
+        call(leaf)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        call(leaf)
+    with pytest.raises(ValueError, match="CUDA"):
+        call(lambda *s, dtype=BF: leaf(*s, dtype=dtype).detach())
