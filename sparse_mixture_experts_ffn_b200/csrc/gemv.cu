@@ -2,9 +2,10 @@
 //
 //   y[r, n] = act(sum_k x[r, k] W[e, n, k] + bias[n]) + residual[r, n]
 //
-// With at most eight rows for a weight HBM bounds the call, and the set-up and hand-overs of a
-// tcgen05 tile are most of its time (4 x 4096 x 4096: 12.9 us there, 9.6 here, 5.1 at the rate of
-// memory; 16 x 11264 x 4096, in two passes of eight rows: 24.4 there, 33.3 here).  Here warps read the weights straight into registers, and nothing is set up.
+// With few rows to a weight HBM bounds the call, and the set-up and hand-overs of a tcgen05 tile are
+// most of its time (4 x 4096 x 4096: 12.9 us there, 9.6 here, 5.1 at the rate of memory).  Here warps read
+// the weights straight into registers, and nothing is set up.  Weights pass once for every eight rows of
+// an expert, however many it has; which calls come here is choose_gemv()'s rule (ops.h).
 //
 // bf16: a warp takes 16 features.  Each lane reads 16-byte pieces of two weight rows and of one row
 // of x, in the places that make them operands of mma.m16n8k16 as they are (the order of the
@@ -15,7 +16,8 @@
 // In both, the warps of a block share the reduction where there would be too few of them.  fp32
 // sums in a fixed order.
 //
-// Grouped: a block takes one row as the first of up to eight of its expert's rows, finds the expert by looking at all offsets at once, and leaves if the row is not a first one.
+// Grouped: a block takes one row as the first of up to eight of its expert's rows, finds the expert by
+// looking at all offsets at once, and leaves if the row is not a first one.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -89,28 +91,21 @@ __device__ __forceinline__ void finish(const GemvParams<T>& p, int r, int n, flo
   p.y[at] = from_f32<T>(z);
 }
 
-// V consecutive values that are read once: not kept in L1, where x is
-template <typename T, int V>
+// V consecutive values; those of a weight are read once and not kept in L1, where x is
+template <int V>
 struct Piece {
-  uint4 q;
-  __device__ __forceinline__ void load(const T* p) {
-    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
+  float4 q;
+  __device__ __forceinline__ void load(const float* p) {
+    asm volatile("ld.global.nc.L1::no_allocate.L2::256B.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(q.x), "=f"(q.y), "=f"(q.z), "=f"(q.w)
                  : "l"(p));
   }
-  __device__ __forceinline__ void keep(const T* p) { q = __ldg(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void zero() { q = make_uint4(0, 0, 0, 0); }
-  __device__ __forceinline__ float at(int i) const {
-    if constexpr (sizeof(T) == 4) {
-      return __uint_as_float(i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w);
-    } else {
-      const uint32_t w = i < 2 ? q.x : i < 4 ? q.y : i < 6 ? q.z : q.w;
-      return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
-    }
-  }
+  __device__ __forceinline__ void keep(const float* p) { q = __ldg(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void zero() { q = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+  __device__ __forceinline__ float at(int i) const { return i == 0 ? q.x : i == 1 ? q.y : i == 2 ? q.z : q.w; }
 };
 template <>
-struct Piece<float, 1> {  // fp32 rows that are not multiples of 16 bytes
+struct Piece<1> {  // rows that are not multiples of 16 bytes
   float v;
   __device__ __forceinline__ void load(const float* p) { v = __ldg(p); }
   __device__ __forceinline__ void keep(const float* p) { v = __ldg(p); }
@@ -119,8 +114,8 @@ struct Piece<float, 1> {  // fp32 rows that are not multiples of 16 bytes
 };
 
 // the next kU pieces of both weight rows, from k on
-template <typename T, int V, int U>
-__device__ __forceinline__ void fetch(Piece<T, V> (*a)[kF], const T* const* w, int k, int step, int K) {
+template <int V, int U>
+__device__ __forceinline__ void fetch(Piece<V> (*a)[kF], const float* const* w, int k, int step, int K) {
 #pragma unroll
   for (int u = 0; u < U; ++u)
 #pragma unroll
@@ -131,18 +126,18 @@ __device__ __forceinline__ void fetch(Piece<T, V> (*a)[kF], const T* const* w, i
 }
 
 // ROWS: rows computed (a block with fewer repeats its last one)
-template <typename T, int V, int ROWS>
-__device__ __forceinline__ void sum_rows(const T* const* w, const T* const* x, int k, int step, int K,
+template <int V, int ROWS>
+__device__ __forceinline__ void sum_rows(const float* const* w, const float* const* x, int k, int step, int K,
                                          float (*acc)[kRows]) {
   constexpr int kU = 4;
-  Piece<T, V> a[kU][kF], next[kU][kF];
-  fetch<T, V, kU>(a, w, k, step, K);
+  Piece<V> a[kU][kF], next[kU][kF];
+  fetch<V, kU>(a, w, k, step, K);
   for (; k < K; k += kU * step) {
-    fetch<T, V, kU>(next, w, k + kU * step, step, K);
+    fetch<V, kU>(next, w, k + kU * step, step, K);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       if (k + u * step < K) {
-        Piece<T, V> b[ROWS];
+        Piece<V> b[ROWS];
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) b[i].keep(x[i] + k + u * step);
 #pragma unroll
@@ -160,30 +155,30 @@ __device__ __forceinline__ void sum_rows(const T* const* w, const T* const* x, i
   }
 }
 
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) gemv_kernel(const GemvParams<T> p) {
+template <int V>
+__global__ void __launch_bounds__(kThreads) gemv_f32_kernel(const GemvParams<float> p) {
   __shared__ int found;
   __shared__ float part[kWarps][kF * kRows];
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int r0, rows, e;
-  if (!find_rows<T, kRows, kThreads>(p, &found, r0, rows, e)) return;
+  if (!find_rows<float, kRows, kThreads>(p, &found, r0, rows, e)) return;
   const int fw = warp / p.ks, kw = warp % p.ks;
   const int n0 = (static_cast<int>(blockIdx.x) * (kWarps / p.ks) + fw) * kF;
   // features and rows past the end repeat the last one; their sums are not stored
-  const T* w[kF];
-  const T* x[kRows];
+  const float* w[kF];
+  const float* x[kRows];
 #pragma unroll
   for (int f = 0; f < kF; ++f) w[f] = p.W + (static_cast<int64_t>(e) * p.N + min(n0 + f, p.N - 1)) * p.K;
 #pragma unroll
   for (int i = 0; i < kRows; ++i) x[i] = p.x + static_cast<int64_t>(r0 + min(i, rows - 1)) * p.K;
   float acc[kF][kRows] = {};
   const int step = 32 * V * p.ks, k0 = (kw * 32 + lane) * V;
-  if (rows == 1) sum_rows<T, V, 1>(w, x, k0, step, p.K, acc);
-  else if (rows == 2) sum_rows<T, V, 2>(w, x, k0, step, p.K, acc);
-  else if (rows <= 4) sum_rows<T, V, 4>(w, x, k0, step, p.K, acc);
-  else sum_rows<T, V, kRows>(w, x, k0, step, p.K, acc);
+  if (rows == 1) sum_rows<V, 1>(w, x, k0, step, p.K, acc);
+  else if (rows == 2) sum_rows<V, 2>(w, x, k0, step, p.K, acc);
+  else if (rows <= 4) sum_rows<V, 4>(w, x, k0, step, p.K, acc);
+  else sum_rows<V, kRows>(w, x, k0, step, p.K, acc);
   float mine = 0.0f;  // lane f * kRows + i: the sum of feature f, row i
 #pragma unroll
   for (int f = 0; f < kF; ++f)
@@ -332,7 +327,7 @@ cudaError_t launch_f32(const GemmArgs& a, cudaStream_t st) {
   // three blocks an SM, each lane with 16 pieces on their way, keep memory busy
   const dim3 grid = grid_of(a, kRows, kWarps, kF, 32 * V, static_cast<int64_t>(a.num_sms) * 3, p.ks);
   count_launches(1);
-  return launch_pdl(gemv_kernel<float, V>, grid, dim3(kThreads), 0, st, p);
+  return launch_pdl(gemv_f32_kernel<V>, grid, dim3(kThreads), 0, st, p);
 }
 
 }  // namespace
