@@ -21,9 +21,10 @@
  *     streams (moe_linear_backward: each with a workspace of its own);
  *   - results do not depend on timing: no atomics, sums in a fixed order;
  *   - all sums are held in fp32 (bf16 products on the tensor cores, which cut off below 2^-23
- *     of the running sum, in parts of at most 16384 terms: within 2^-13 of the sum of the
- *     terms' magnitudes, however many there are); a bf16 result is rounded once, at the end, except
- *     the gradient dz of moe_linear_backward, which is rounded to bf16 between its two products;
+ *     of the running sum, in parts of at most 16384 terms that are added in fp32: within 2^-13,
+ *     and 2^-24 for each part, of the sum of the terms' magnitudes); a bf16 result is rounded once,
+ *     at the end, except the gradient dz of moe_linear_backward, which is rounded to bf16 between
+ *     its two products;
  *   - the return value reports argument validation and launch errors; errors found on the
  *     device (offsets out of range, a bounded wait that timed out) go to a per-device status
  *     word that moe_ops_check_status() reads and clears.
@@ -60,7 +61,8 @@ typedef struct {
  *   moe_grouped_gemm_wgrad  dW[e] [E, N, K]  = sum over the rows r of e of dy[r]^T x[r]
  * Rows outside [offsets[0], offsets[E]) are neither read for a result nor written, whatever
  * they hold; dW[e] of an expert without rows is zero.  An expert whose offsets are out of
- * order or out of [0, R] counts as empty, and MOE_ERR_DEVICE_BOUNDS is recorded. */
+ * order or out of [0, R] counts as empty, and MOE_ERR_DEVICE_BOUNDS is recorded; what the
+ * result then holds of the other experts' rows is not specified. */
 MOE_API moe_status moe_grouped_gemm(const moe_gemm_shape* shape, const void* x, const void* W, const int32_t* offsets,
                                     void* y, void* stream);
 MOE_API moe_status moe_grouped_gemm_dgrad(const moe_gemm_shape* shape, const void* dy, const void* W,
@@ -110,7 +112,8 @@ MOE_API moe_status moe_swiglu_backward(int64_t R, int32_t I, int32_t dtype, cons
 /* Synchronises `stream`, then returns and clears the current device's status word: the first
  * error that a kernel of the calls above recorded since the last call of this function
  * (MOE_ERR_DEVICE_BOUNDS, MOE_ERR_DEVICE_TIMEOUT), MOE_OK, or MOE_ERR_CUDA if the stream
- * itself reports an error.  The word is shared by all streams of the device. */
+ * itself reports an error.  The word is shared by all streams of the device; it is read and
+ * cleared in one step, so that what is recorded meanwhile is left for the next call. */
 MOE_API moe_status moe_ops_check_status(void* stream);
 
 #ifdef __cplusplus

@@ -33,12 +33,22 @@ cudaError_t launch_gemm_bf16(const GemmArgs& a, cudaStream_t st);
 cudaError_t launch_gemm_f32(const GemmArgs& a, cudaStream_t st);
 // The forward product for a few rows: weights pass once for every eight rows of an expert.
 cudaError_t launch_gemv(const GemmArgs& a, bool bf16, cudaStream_t st);
-// Measured against the tiles (the sizes of the groups are not known here, only their average):
-//   bf16, 16 experts of 1024 x 1024: 1 row each 6.3 us against 9.4, 4 rows 9.5 against 9.4, 8 rows
-//   11.9 against 9.3; a linear layer of 2048 x 2048: 8 rows 4.0 against 8.7 for 16;
-//   fp32, 16 experts of 1024 x 1024: 1 row each 13.6 us against 90.9 (row tiles are mostly
-//   padding), 8 rows 46.5 against 114.7, 16 rows 89.8 against 94.1 (of 512 x 512, 64 experts: 135
-//   against 65); a linear layer of 2048 x 2048: 8 rows 11.4 against 26.7, 16 rows 19.1 against 27.1.
+// Measured against the tiles, in us, with the rows spread evenly / all with one expert (the sizes of the
+// groups are not known here, only their average):
+//                                     few-row kernel   tiles
+//   bf16, 288 of 2560 x 4096, 1 row     879 / 102    882 / 27
+//                             2 rows    887 / 189    911 / 51
+//         288 of 512 x 512,   2 rows     31 / 15      33 / 8
+//                             4 rows     35 / 24      33 / 8
+//   fp32, 16 of 1024 x 1024,  1 row      12 / 8       90 / 42 (row tiles are mostly padding)
+//                             8 rows     39 / 39     111 / 65
+//         288 of 1024 x 1024, 8 rows    716 / 694    965 / 287
+//         288 of 512 x 512,   8 rows    280 / 279    251 / 83
+//         64 of 512 x 512,    16 rows   109 / 108     65 / 51
+//   linear layer, bf16, 8 rows of 2048 x 2048 4.1 and 8.5, 16 rows of 11264 x 4096 32 and 24;
+//                 fp32, 16 rows of 2048 x 2048 12 and 27
+// So the rule is for spread rows.  With all of them at one expert the few-row kernel never takes
+// longer than with as many spread, but up to five times as long as the tiles would.
 inline bool choose_gemv(const GemmArgs& a, bool bf16) {
   if (a.pass != kFwd) return false;
   if (!a.offsets) return a.R <= (bf16 ? 8 : 16);
